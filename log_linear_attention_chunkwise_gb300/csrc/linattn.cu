@@ -60,7 +60,7 @@ struct Cost {
 // How a call runs.  Its walks (`walks` of them, counted in heads) go over whole
 // sequences, or in segments side by side whose incoming states `passes` state
 // passes and the scan form first: the cheapest cut into at most kLinMaxSeg
-// segments of whole tiles.  A state that is handed out (`state`) comes with
+// segments of whole tiles (more where bf16 walks of kLinWalkTiles need them).  A state that is handed out (`state`) comes with
 // split walks from the scan.  Whole walks in fp32 hand it out themselves;
 // those in bf16, whose own state is only as accurate as their output, leave it
 // to one state pass behind them.
@@ -75,13 +75,16 @@ Plan plan(int B, int H, int T, int dk, int dv, lla_dtype dt, int jobs, int passe
     const long long BH = (long long)B * H, walks = jobs * BH;
     const int tiles = tiles_of(T);
     const Cost c(dk, dv, dt);
+    const bool tc = linattn_tc_supported(dt);
+    const int fewest = tc ? (tiles + kLinWalkTiles - 1) / kLinWalkTiles : 1;
     Segments best{1, tiles};
-    double least = state && linattn_tc_supported(dt) ? c.behind(walks, BH, tiles) : c.walk(walks, best);
-    for (int n = 2; n <= kLinMaxSeg && n <= tiles && walks * (n - 1) < 4LL * c.sms; n++) {
+    double least = state && tc ? c.behind(walks, BH, tiles) : c.walk(walks, best);
+    for (int n = fewest > 2 ? fewest : 2;
+         n == fewest || (n <= kLinMaxSeg && n <= tiles && walks * (n - 1) < 4LL * c.sms); n++) {
         const Segments s{n, (tiles + n - 1) / n};
-        if ((tiles + s.tiles - 1) / s.tiles != n) continue;
+        if ((tiles + s.tiles - 1) / s.tiles != n) continue;  // never of the fewest
         const double cost = c.walk(walks, s) + c.states(passes * BH, s);
-        if (cost < least) {
+        if (cost < least || n == fewest) {
             least = cost;
             best = s;
         }

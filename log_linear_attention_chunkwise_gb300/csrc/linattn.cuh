@@ -17,7 +17,13 @@
 namespace lla {
 
 constexpr int kLinTile = 128;     // tokens per tile; segments are whole tiles
-constexpr int kLinMaxSeg = 256;   // segments of one sequence
+constexpr int kLinMaxSeg = 256;   // segments of one sequence, where it is not cut for kLinWalkTiles
+// Tiles of one walk on the tensor cores.  Its state stays in one accumulator, which is not rounded to nearest: with
+// a = 1 and terms of one sign it falls short by about 2.3e-6 a tile (measured).  256 tiles hold that to 6e-4, against
+// the 2^-9 and more of the state operand's own rounding, and the next segment starts from a state of fp32 accuracy;
+// whole walks of 4096 tiles were 2.8e-3 short, growing with T.  152 heads of 65536 tokens, D = 128, without a state:
+// 1513 us whole, 2410 so (a pass over k and v for the states); up to 32768 tokens nothing is cut for it.
+constexpr int kLinWalkTiles = 256;
 constexpr int kLinMaxJobs = 3;
 
 struct LinJob {

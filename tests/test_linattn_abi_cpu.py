@@ -52,6 +52,16 @@ def test_workspace_queries(lib):
     assert n >= 2 * 3 * 100 * 32 * 2 + lib.lla_layer_norm_bwd_workspace_bytes(2, 3, 100, 32, 1)
 
 
+def test_long_walks_are_cut(lib):
+    # a walk's accumulator takes 256 tiles at most, however many heads there are; fp32 sums need no such cut
+    f, b = lib.lla_linattn_fwd_workspace_bytes, lib.lla_linattn_bwd_workspace_bytes
+    for tiles in (512, 513, 131072):
+        n = (tiles + 255) // 256
+        assert f(4, 76, 128 * tiles, 128, 64, 1) >= 4 * 76 * n * 128 * 64 * 4
+        assert b(4, 76, 128 * tiles, 128, 64, 1) >= 2 * 4 * 76 * n * 128 * 64 * 4
+    assert f(4, 76, 65536, 128, 64, 0) == 0
+
+
 def test_bwd_refusals(lib):
     def bwd(q=P, do=P, dq=P, dv=P, ld=P, si=NULL, dso=NULL, dsi=NULL, B=1, T=64, dk=64, dt=1, ws=P, wsb=BIG):
         return lib.lla_linattn_bwd(q, P, P, ld, NULL, si, do, dso, dq, P, dv, dsi, B, 1, T, dk, 64, dt, 0, ws, wsb,
