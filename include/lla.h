@@ -415,7 +415,8 @@ lla_status lla_lambda_mlp(const void *d, const float *W1, const float *W2,
  *     S_t = a S_{t-1} + k_t v_t^T,   o_t = q_t S_t,   S_{-1} = state_in (or 0)
  *         = sum_{s<=t} a^(t-s) (q_t . k_s) v_s + a^(t+1) q_t state_in.
  * log_decay <= 0 is intended (-inf, a = 0, is allowed: every token sees only
- * itself); it is a constant of the model and takes no gradient here.
+ * itself; with NaN every output of the head's tokens is NaN); it is a constant
+ * of the model and takes no gradient here.
  *
  * lla_linattn_fwd: whole prompts, O(T), in tiles of 128 tokens; long sequences
  * of few heads are cut into segments whose states are formed first and joined.

@@ -51,10 +51,11 @@ struct LinWalk {
 
 // exp(ld * n) for n >= 0.  The product's rounding error is carried into the
 // result (|ld n| can be large), and ld is held above -1e4, where every power
-// but the zeroth is 0 in fp32 anyway, so that 0 * ld is 0 for any ld.
+// but the zeroth is 0 in fp32 anyway, so that 0 * ld is 0 for any ld.  A NaN
+// passes the comparison and every power of it is NaN.
 __device__ __forceinline__ float decay_pow(float ld, int n)
 {
-    ld = fmaxf(ld, -1e4f);
+    ld = ld < -1e4f ? -1e4f : ld;
     const float p = ld * (float)n;
     const float e = fmaf(ld, (float)n, -p);
     return expf(p) * (1.f + e);

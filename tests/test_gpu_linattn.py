@@ -453,3 +453,30 @@ def test_long_sums_without_decay(T, d, cuda_device):
     check(dv[:, :, :part], v1, "dv")
     del dq, dk, dv, k1, v1, first, last
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("T,d,dtype", [(300, 128, BF16), (300, 64, BF16), (2000, 128, BF16), (300, 32, F32), (1700, 64, F32)])
+def test_a_decay_that_is_nan_shows(T, d, dtype, cuda_device):
+    """Every output of such a head is NaN (a sequence without tokens hands its state through), no other head's changes."""
+    x = dev(lin_inputs(2, 3, T, d, d, dtype, seed=8))
+    nan = x["log_decay"].clone()
+    nan[1] = float("nan")
+    lens = torch.tensor([T - 7, 0], dtype=torch.int32, device="cuda")
+    token = [x[n][:, :, 0].contiguous() for n in "qkv"]
+
+    def step(ld):
+        pool = x["state"].clone()
+        fwd = binding.linattn_fwd(x["q"], x["k"], x["v"], ld, lens=lens, state_in=x["state"], return_state=True)
+        bwd = binding.linattn_bwd(x["q"], x["k"], x["v"], ld, x["dout"], lens=lens, state_in=x["state"],
+                                  dstate_out=x["dstate"], return_dstate=True)
+        return dict(zip(("out", "state", "dq", "dk", "dv", "dstate"), fwd + bwd)), (
+            binding.linattn_decode_step(pool, *token, ld), pool)
+
+    (rows, tok), (want, want_tok) = step(nan), step(x["log_decay"])
+    for name, g in rows.items():
+        at = g[0, 1] if "state" in name else g[0, 1, :T - 7]
+        assert bool(at.isnan().all()), name
+        assert torch.equal(g[:, [0, 2]], want[name][:, [0, 2]]) and torch.equal(g[1], want[name][1]), name
+    assert torch.equal(rows["state"][1], x["state"][1]) and torch.equal(rows["dstate"][1], x["dstate"][1])
+    for g, w in zip(tok, want_tok):
+        assert bool(g[:, 1].isnan().all()) and torch.equal(g[:, [0, 2]], w[:, [0, 2]])
