@@ -440,6 +440,8 @@ lla_status lla_lambda_mlp(const void *d, const float *W1, const float *W2,
  * by then.  state_out keeps fp32 accuracy.  A value that is not finite in
  * row s of k or v may reach the outputs of the other tokens of its 128-token
  * tile, not only those of the later tokens.
+ * out may overlap neither an input nor state_out, and state_out no input but
+ * state_in itself (refused: other CTAs still read there).
  * Supported: dk, dv in {16,32,64,128}, any T from 0 to 2^24, B*H <= 65535.
  * Pointers 16-byte aligned; workspace >= lla_linattn_fwd_workspace_bytes(...)
  * bytes (where that is 0 it may be NULL; enough with and without state_out),
@@ -462,8 +464,8 @@ lla_status lla_linattn_fwd(const void *q, const void *k, const void *v, const fl
  *     dv_s = sum_{t>=s} a^(t-s) (q_t . k_s) dout_t + a^(n-1-s) k_s dstate_out
  *     dstate_in = sum_t a^(t+1) q_t dout_t^T + a^n dstate_out,   n = lens[b] or T.
  *   dout [B,H,T,dv] in dt; dq, dk [B,H,T,dk], dv [B,H,T,dv] in dt; dstate_in
- *   [B,H,dk,dv] fp32, nullable, not the same buffer as dstate_out or state_in
- *   (refused).
+ *   [B,H,dk,dv] fp32, nullable.  The outputs overlap neither one another nor an
+ *   input (refused).
  * Rows behind lens[b] stay as they were in dq, dk, dv.  Shapes, lengths,
  * accuracy, errors as lla_linattn_fwd; workspace as its own query says.
  */
@@ -485,6 +487,7 @@ lla_status lla_linattn_bwd(const void *q, const void *k, const void *v, const fl
  *     skipped, its state left as it was, and 1 + b is stored in *device_error
  *     (one of the b when several).  Rows of out of padded and of skipped
  *     sequences stay as they were, or are set to 0 with clear_skipped.
+ * state and out overlap neither each other nor q, k, v (refused).
  * Supported: dk, dv in {16,32,64,128}; B <= 65535; pool, H >= 0.
  */
 lla_status lla_linattn_decode_step(float *state, const void *q, const void *k, const void *v,
@@ -516,10 +519,11 @@ lla_status lla_zero_padding(void *const *rows, const int32_t *row_bytes, const i
  *     dx = rstd (g - avg(g) - h avg(g h)),  dweight = sum over b, t of dy h,
  *     dbias = sum over b, t of dy.
  *   mean, rstd as the forward wrote them; dx [B,H,T,N] in dt, may be the same
- *   buffer as dy; dweight, dbias [H,N] fp32, nullable, overwritten; sums in a
+ *   buffer as dy or x; dweight, dbias [H,N] fp32, nullable, overwritten; sums in a
  *   fixed order (the same bits every time).
  * Supported: 1 <= N <= 16384, B*H <= 65535, any T >= 0, eps >= 0.  x, dy, y,
- * dx, weight, bias 16-byte aligned.  Empty calls write zero dweight and dbias.
+ * dx, weight, bias 16-byte aligned.  Beyond the buffers that may be the same,
+ * no output overlaps another one or an input (refused).  Empty calls write zero dweight and dbias.
  */
 lla_status lla_layer_norm_fwd(const void *x, const float *weight, const float *bias,
                               const int32_t *lens, void *y, float *mean, float *rstd, int B, int H,

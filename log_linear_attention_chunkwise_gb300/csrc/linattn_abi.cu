@@ -27,6 +27,63 @@ template <typename... P> bool aligned(P... p) { return ((((uintptr_t)p & 15u) ==
 
 size_t elt(lla_dtype dt) { return dt == LLA_BF16 ? 2 : 4; }
 
+// A buffer of a call.  An output that overlaps what other CTAs still read (or write) would be a race: refused.
+struct Span {
+    const void *p;
+    size_t bytes;
+};
+
+bool overlap(const Span &a, const Span &b)
+{
+    const uintptr_t x = (uintptr_t)a.p, y = (uintptr_t)b.p;
+    return x != 0 && y != 0 && x < y + b.bytes && y < x + a.bytes;
+}
+
+// no output overlaps another one or an input
+bool apart(std::initializer_list<Span> outputs, std::initializer_list<Span> inputs)
+{
+    for (const Span *o = outputs.begin(); o != outputs.end(); o++) {
+        for (const Span *p = outputs.begin(); p != o; p++)
+            if (overlap(*o, *p)) return false;
+        for (const Span &i : inputs)
+            if (overlap(*o, i)) return false;
+    }
+    return true;
+}
+
+// the same buffer, or no common byte
+bool same_or_apart(const Span &a, const Span &b) { return a.p == b.p || !overlap(a, b); }
+
+// the outputs of lla_linattn_fwd
+bool fwd_apart(const void *q, const void *k, const void *v, const float *state_in, const void *out,
+               const float *state_out, int B, int H, int T, int dk, int dv, lla_dtype dt)
+{
+    const size_t rows = (size_t)B * H * T, bk = rows * dk * elt(dt), bv = rows * dv * elt(dt);
+    const size_t bs = (size_t)B * H * dk * dv * 4;
+    return apart({{out, bv}, {state_out, bs}}, {{q, bk}, {k, bk}, {v, bv}}) && !overlap({out, bv}, {state_in, bs}) &&
+           same_or_apart({state_out, bs}, {state_in, bs});
+}
+
+// the outputs of lla_layer_norm_fwd
+bool norm_fwd_apart(const void *x, const float *weight, const float *bias, const void *y, const float *mean,
+                    const float *rstd, int B, int H, int T, int N, lla_dtype dt)
+{
+    const size_t rows = (size_t)B * H * T, bx = rows * N * elt(dt), bw = (size_t)H * N * 4;
+    return apart({{y, bx}, {mean, rows * 4}, {rstd, rows * 4}}, {{weight, bw}, {bias, bw}}) &&
+           apart({{mean, rows * 4}, {rstd, rows * 4}}, {{x, bx}}) && same_or_apart({y, bx}, {x, bx});
+}
+
+// the outputs of lla_linattn_bwd
+bool bwd_apart(const void *q, const void *k, const void *v, const float *state_in, const void *dout,
+               const float *dstate_out, const void *dq, const void *dk, const void *dv, const float *dstate_in, int B,
+               int H, int T, int dk_dim, int dv_dim, lla_dtype dt)
+{
+    const size_t rows = (size_t)B * H * T, bk = rows * dk_dim * elt(dt), bv = rows * dv_dim * elt(dt);
+    const size_t bs = (size_t)B * H * dk_dim * dv_dim * 4;
+    return apart({{dq, bk}, {dk, bk}, {dv, bv}, {dstate_in, bs}},
+                 {{q, bk}, {k, bk}, {v, bv}, {dout, bv}, {state_in, bs}, {dstate_out, bs}});
+}
+
 lla_status lin_shape_status(int B, int H, int T, int dk, int dv, lla_dtype dt)
 {
     if (B < 0 || H < 0 || T < 0 || !is_dtype(dt)) return LLA_ERR_INVALID_ARGUMENT;
@@ -94,6 +151,7 @@ lla_status lla_linattn_fwd(const void *q, const void *k, const void *v, const fl
     if (T > 0 && !good(q, k, v, (const void *)out)) return LLA_ERR_INVALID_ARGUMENT;
     st = workspace_status(workspace, workspace_bytes, lla_linattn_fwd_workspace_bytes(B, H, T, dk, dv, dt));
     if (st != LLA_OK) return st;
+    if (!fwd_apart(q, k, v, state_in, out, state_out, B, H, T, dk, dv, dt)) return LLA_ERR_INVALID_ARGUMENT;
     clear_padding = clear_padding && lens != nullptr;
     if (clear_padding) {
         st = clear(lens, B, H, T, stream, {{out, dv * elt(dt), true}, {state_out, (size_t)dk * dv * 4, false}});
@@ -123,13 +181,14 @@ lla_status lla_linattn_bwd(const void *q, const void *k, const void *v, const fl
     if (st != LLA_OK) return st;
     if ((long long)B * H == 0) return LLA_OK;
     if (!log_decay || !aligned(state_in, dstate_out, dstate_in)) return LLA_ERR_INVALID_ARGUMENT;
-    // dk is formed from dstate_out, dq from state_in, while dstate_in is written
-    if (dstate_in != nullptr && (dstate_in == dstate_out || dstate_in == state_in)) return LLA_ERR_INVALID_ARGUMENT;
     if (T > 0 && !good(q, k, v, dout, (const void *)dq, (const void *)dk, (const void *)dv))
         return LLA_ERR_INVALID_ARGUMENT;
     st = workspace_status(workspace, workspace_bytes,
                           lla_linattn_bwd_workspace_bytes(B, H, T, dk_dim, dv_dim, dt));
     if (st != LLA_OK) return st;
+    // dk is formed from dstate_out, dq from state_in, while dstate_in is written
+    if (!bwd_apart(q, k, v, state_in, dout, dstate_out, dq, dk, dv, dstate_in, B, H, T, dk_dim, dv_dim, dt))
+        return LLA_ERR_INVALID_ARGUMENT;
     clear_padding = clear_padding && lens != nullptr;
     if (clear_padding) {
         const size_t rk = dk_dim * elt(dt), rv = dv_dim * elt(dt);
@@ -156,6 +215,10 @@ lla_status lla_linattn_decode_step(float *state, const void *q, const void *k, c
     if ((long long)B * H == 0) return LLA_OK;
     if (slots == nullptr && pool < B) return LLA_ERR_INVALID_ARGUMENT;
     if (!log_decay || !good((const void *)state, q, k, v, (const void *)out)) return LLA_ERR_INVALID_ARGUMENT;
+    const size_t heads = (size_t)B * H;
+    if (!apart({{state, (size_t)pool * H * dk * dv * 4}, {out, heads * dv * 4}},
+               {{q, heads * dk * elt(dt)}, {k, heads * dk * elt(dt)}, {v, heads * dv * elt(dt)}}))
+        return LLA_ERR_INVALID_ARGUMENT;
     LinDecodeArgs A;
     A.state = state; A.q = q; A.k = k; A.v = v; A.log_decay = log_decay; A.slots = slots; A.out = out;
     A.pool = pool; A.B = B; A.H = H; A.dk = dk; A.dv = dv; A.dt = dt; A.clear_skipped = clear_skipped;
@@ -194,6 +257,7 @@ lla_status lla_layer_norm_fwd(const void *x, const float *weight, const float *b
     if (!(eps >= 0.f) || isinf(eps)) return LLA_ERR_INVALID_ARGUMENT;
     if ((long long)B * H * T == 0) return LLA_OK;
     if (!good(x, (const void *)y) || !aligned(weight, bias)) return LLA_ERR_INVALID_ARGUMENT;
+    if (!norm_fwd_apart(x, weight, bias, y, mean, rstd, B, H, T, N, dt)) return LLA_ERR_INVALID_ARGUMENT;
     if (clear_padding && lens != nullptr) {
         st = clear(lens, B, H, T, stream, {{y, N * elt(dt), true}, {mean, 4, true}, {rstd, 4, true}});
         if (st != LLA_OK) return st;
@@ -230,6 +294,11 @@ lla_status lla_layer_norm_bwd(const void *x, const float *weight, const float *m
         st = workspace_status(workspace, workspace_bytes, layer_norm_bwd_workspace_bytes(B, H, T, N, dt));
         if (st != LLA_OK) return st;
     }
+    const size_t rows = (size_t)B * H * T, bx = rows * N * elt(dt), bw = (size_t)H * N * 4;
+    if (!apart({{dx, bx}, {dweight, bw}, {dbias, bw}}, {{weight, bw}, {mean, rows * 4}, {rstd, rows * 4}}) ||
+        !apart({{dweight, bw}, {dbias, bw}}, {{x, bx}, {dy, bx}}) || !same_or_apart({dx, bx}, {dy, bx}) ||
+        !same_or_apart({dx, bx}, {x, bx}))
+        return LLA_ERR_INVALID_ARGUMENT;
     if (clear_padding && lens != nullptr) {
         st = clear(lens, B, H, T, stream, {{dx, N * elt(dt), true}});
         if (st != LLA_OK) return st;
@@ -253,6 +322,10 @@ lla_status lla_linattn_norm_fwd(const void *q, const void *k, const void *v, con
     if (st != LLA_OK) return st;
     if (!(eps >= 0.f) || isinf(eps)) return LLA_ERR_INVALID_ARGUMENT;
     if ((long long)B * H * T > 0 && (!good((const void *)o, (const void *)y) || !aligned(weight, bias)))
+        return LLA_ERR_INVALID_ARGUMENT;
+    const size_t rows = (size_t)B * H * T, bs = (size_t)B * H * dk * dv * 4;
+    if (!norm_fwd_apart(o, weight, bias, y, mean, rstd, B, H, T, dv, dt) ||
+        !apart({{state_out, bs}}, {{y, rows * dv * elt(dt)}, {mean, rows * 4}, {rstd, rows * 4}}))
         return LLA_ERR_INVALID_ARGUMENT;
     st = lla_linattn_fwd(q, k, v, log_decay, lens, state_in, o, state_out, B, H, T, dk, dv, dt, clear_padding,
                          workspace, workspace_bytes, device_error, stream);
@@ -283,7 +356,6 @@ lla_status lla_linattn_norm_bwd(const void *q, const void *k, const void *v, con
     // every check of both calls before the first is enqueued
     if ((long long)B * H > 0) {
         if (!log_decay || !aligned(state_in, dstate_out, dstate_in)) return LLA_ERR_INVALID_ARGUMENT;
-        if (dstate_in != nullptr && (dstate_in == dstate_out || dstate_in == state_in)) return LLA_ERR_INVALID_ARGUMENT;
     }
     if ((long long)B * H * T > 0) {
         if (!good(q, k, v, o, dy, (const void *)dq, (const void *)dk, (const void *)dv) || !mean || !rstd ||
@@ -293,6 +365,12 @@ lla_status lla_linattn_norm_bwd(const void *q, const void *k, const void *v, con
                               lla_linattn_norm_bwd_workspace_bytes(B, H, T, dk_dim, dv_dim, dt));
         if (st != LLA_OK) return st;
     }
+    const size_t rows = (size_t)B * H * T, bk = rows * dk_dim * elt(dt), bv = rows * dv_dim * elt(dt);
+    const size_t bw = (size_t)H * dv_dim * 4, bs = (size_t)B * H * dk_dim * dv_dim * 4;
+    if (!bwd_apart(q, k, v, state_in, workspace, dstate_out, dq, dk, dv, dstate_in, B, H, T, dk_dim, dv_dim, dt) ||
+        !apart({{dweight, bw}, {dbias, bw}}, {{q, bk}, {k, bk}, {v, bv}, {dq, bk}, {dk, bk}, {dv, bv}, {dstate_in, bs},
+                                              {state_in, bs}, {dstate_out, bs}}))
+        return LLA_ERR_INVALID_ARGUMENT;
     const size_t off = (long long)B * H * T > 0 ? align_up((size_t)B * H * T * dv_dim * elt(dt), 256) : 0;
     char *rest = (char *)workspace + off;
     const size_t rest_bytes = off > 0 ? workspace_bytes - off : workspace_bytes;

@@ -157,3 +157,92 @@ CALLS = {
 def test_host_tensors_are_refused(name, lib):
     with pytest.raises(ValueError, match="CUDA tensor"):
         CALLS[name]()
+
+
+# ---- outputs that overlap what the call reads, or one another
+
+def at(i, shift=0):
+    return ctypes.c_void_p((i << 40) + shift)
+
+
+N_ROWS, N_STATE = 2 * 3 * 100 * 64 * 2, 2 * 3 * 64 * 64 * 4  # bytes of [2,3,100,64] bf16, of the states
+
+
+def spans(base, size):
+    """The buffer itself, and overlaps by its last and by its first 16 bytes."""
+    return [at(base), at(base, size - 16), at(base, 16 - size)]
+
+
+def test_fwd_overlaps_are_refused(lib):
+    def fwd(out=at(4), so=at(6), norm=False, y=at(7), mean=at(8), rstd=at(9)):
+        a = (at(1), at(2), at(3), at(10), NULL, at(5))
+        if norm:
+            return lib.lla_linattn_norm_fwd(*a, at(11), at(12), 1e-5, out, y, mean, rstd, so, 2, 3, 100, 64, 64, 1, 0,
+                                            at(13), BIG, NULL, NULL)
+        return lib.lla_linattn_fwd(*a, out, so, 2, 3, 100, 64, 64, 1, 0, at(13), BIG, NULL, NULL)
+
+    for norm in (False, True):
+        for base, size in ((1, N_ROWS), (2, N_ROWS), (3, N_ROWS), (5, N_STATE)):
+            for p in spans(base, min(size, N_ROWS)):
+                assert fwd(out=p, norm=norm) == ARG, (norm, base)
+        for base in (1, 2, 3, 4):
+            for p in spans(base, N_ROWS):
+                assert fwd(so=p, norm=norm) == ARG, (norm, base)
+        for p in spans(5, N_STATE)[1:]:  # a part of state_in; the whole of it is allowed
+            assert fwd(so=p, norm=norm) == ARG, norm
+    for p in spans(4, N_ROWS)[1:]:       # a part of o; the whole of it is allowed
+        assert fwd(y=p, norm=True) == ARG
+    for kw in (dict(y=at(6)), dict(mean=at(4)), dict(rstd=at(8)), dict(mean=at(7)), dict(y=at(11)), dict(rstd=at(6))):
+        assert fwd(norm=True, **kw) == ARG, kw
+
+
+def test_bwd_overlaps_are_refused(lib):
+    def bwd(norm=False, dw=at(14), db=at(15), **kw):
+        o = {"dq": at(7), "dk": at(8), "dv": at(9), "ds": at(10), **kw}
+        a, tail = (at(1), at(2), at(3), at(11), NULL, at(5)), (2, 3, 100, 64, 64, 1, 0, at(13), BIG, NULL, NULL)
+        if norm:
+            return lib.lla_linattn_norm_bwd(*a, at(16), at(17), at(18), at(19), at(4), at(6), o["dq"], o["dk"], o["dv"],
+                                            dw, db, o["ds"], *tail)
+        return lib.lla_linattn_bwd(*a, at(4), at(6), o["dq"], o["dk"], o["dv"], o["ds"], *tail)
+
+    for norm in (False, True):
+        for name in ("dq", "dk", "dv", "ds"):
+            for base, size in ((1, N_ROWS), (2, N_ROWS), (3, N_ROWS), (5, N_STATE), (6, N_STATE)):
+                for p in spans(base, min(size, N_ROWS)):
+                    assert bwd(norm, **{name: p}) == ARG, (norm, name, base)
+        for a, b in (("dq", 8), ("dk", 9), ("dv", 7), ("ds", 7), ("dq", 10)):
+            assert bwd(norm, **{a: at(b, 32)}) == ARG, (norm, a, b)
+    assert bwd(dq=at(4)) == ARG
+    for kw in (dict(dw=at(15)), dict(dw=at(16)), dict(db=at(4)), dict(dw=at(17)), dict(db=at(1)), dict(dw=at(9))):
+        assert bwd(True, **kw) == ARG, kw
+
+
+def test_norm_overlaps_are_refused(lib):
+    size = 3 * 50 * 100 * 4
+
+    def fwd(y=at(4), mean=at(5), rstd=at(6)):
+        return lib.lla_layer_norm_fwd(at(1), at(2), at(3), NULL, y, mean, rstd, 1, 3, 50, 100, 1e-5, 0, 0, NULL, NULL)
+
+    def bwd(dx=at(6), dw=at(7), db=at(8)):
+        return lib.lla_layer_norm_bwd(at(1), at(2), at(3), at(4), NULL, at(5), dx, dw, db, 1, 3, 50, 100, 0, 0, at(13),
+                                      BIG, NULL, NULL)
+    for p in spans(1, size)[1:]:
+        assert fwd(y=p) == ARG and bwd(dx=p) == ARG
+    for p in spans(5, size)[1:]:
+        assert bwd(dx=p) == ARG
+    for kw in (dict(y=at(2)), dict(y=at(3)), dict(y=at(5)), dict(mean=at(1)), dict(rstd=at(1, 64)), dict(mean=at(6)),
+               dict(mean=at(2))):
+        assert fwd(**kw) == ARG, kw
+    for kw in (dict(dx=at(2)), dict(dx=at(3)), dict(dx=at(4)), dict(dx=at(7)), dict(dw=at(8)), dict(dw=at(1)),
+               dict(db=at(5)), dict(dw=at(3)), dict(db=at(2))):
+        assert bwd(**kw) == ARG, kw
+
+
+def test_decode_overlaps_are_refused(lib):
+    def dec(state=at(1), out=at(5), dt=0):
+        return lib.lla_linattn_decode_step(state, at(2), at(3), at(4), at(6), NULL, out, 4, 2, 3, 64, 64, dt, 0, NULL, NULL)
+    for base, size in ((1, 2 * 3 * 64 * 4), (2, 2 * 3 * 64 * 4), (3, 2 * 3 * 64 * 4), (4, 2 * 3 * 64 * 4)):
+        for p in spans(base, size):
+            assert dec(out=p) == ARG, base
+    for base in (2, 3, 4):
+        assert dec(state=at(base)) == ARG and dec(state=at(base, 256)) == ARG
