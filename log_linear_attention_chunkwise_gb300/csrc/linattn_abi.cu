@@ -214,7 +214,9 @@ lla_status lla_linattn_decode_step(float *state, const void *q, const void *k, c
     if (!is_dim(dk) || !is_dim(dv) || B > 65535 || H > (1 << 24)) return LLA_ERR_UNSUPPORTED_SHAPE;
     if ((long long)B * H == 0) return LLA_OK;
     if (slots == nullptr && pool < B) return LLA_ERR_INVALID_ARGUMENT;
-    if (!log_decay || !good((const void *)state, q, k, v, (const void *)out)) return LLA_ERR_INVALID_ARGUMENT;
+    // an empty pool has no address; its slots are all padding or out of range
+    if (!log_decay || (pool > 0 && !good((const void *)state)) || !good(q, k, v, (const void *)out))
+        return LLA_ERR_INVALID_ARGUMENT;
     const size_t heads = (size_t)B * H;
     if (!apart({{state, (size_t)pool * H * dk * dv * 4}, {out, heads * dv * 4}},
                {{q, heads * dk * elt(dt)}, {k, heads * dk * elt(dt)}, {v, heads * dv * elt(dt)}}))

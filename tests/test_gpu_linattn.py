@@ -480,3 +480,20 @@ def test_a_decay_that_is_nan_shows(T, d, dtype, cuda_device):
     assert torch.equal(rows["state"][1], x["state"][1]) and torch.equal(rows["dstate"][1], x["dstate"][1])
     for g, w in zip(tok, want_tok):
         assert bool(g[:, 1].isnan().all()) and torch.equal(g[:, [0, 2]], w[:, [0, 2]])
+
+
+def test_decode_on_an_empty_pool(cuda_device):
+    """pool = 0: padding only, and any other slot is out of range."""
+    x = dev(lin_inputs(3, 2, 1, 64, 64, BF16, seed=3))
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+
+    def step(slots):
+        return binding.linattn_decode_step(torch.empty((0, 2, 64, 64), device="cuda"), *(x[n][:, :, 0].contiguous() for n in "qkv"),
+                                           x["log_decay"], device_error=err,
+                                           slots=torch.tensor(slots, dtype=torch.int32, device="cuda"))
+
+    assert bool((step([-1, -1, -1]) == 0).all()) and int(err.item()) == 0
+    assert bool((step([-1, 0, -1]) == 0).all()) and int(err.item()) == 2
+    with pytest.raises(binding.LLAError, match="INVALID_ARGUMENT"):  # without slots every sequence needs a state
+        binding.linattn_decode_step(torch.empty((0, 2, 64, 64), device="cuda"), *(x[n][:, :, 0].contiguous() for n in "qkv"),
+                                    x["log_decay"])
