@@ -45,7 +45,7 @@ using namespace sm100;
 constexpr int kTile = 128;       // tokens per tile (MMA M)
 constexpr int kTileLevels = 7;   // levels inside a tile: bit_length(a ^ b) <= 7
 constexpr uint32_t kBlk = kTile * 128;  // one 64-column swizzled block of a 128-row bf16 tile: 16 KB
-constexpr uint32_t kWaitIters = 1u << 22;  // bounded waits (~0.5 s with back-off)
+constexpr uint32_t kWaitIters = 1u << 22;  // bounded waits (~7 s: 1.7 us a poll)
 constexpr uint32_t kWithheldWaitIters = 4096;  // the waits while the test hook withholds a product
 constexpr int kMaxPath = 17;               // levels of a tile index (T <= 2^24, so NT <= 2^17)
 constexpr int kLamMax = 25;                // lambda entries per token: L <= 1 + bit_length(2^24 - 1)
@@ -1214,6 +1214,7 @@ static cudaError_t launch_consumer(const CUtensorMap &mq, const CUtensorMap &mk,
 static std::atomic<int> g_withhold_first_product{0};
 
 void tc_set_withhold_first_product(int enable) { g_withhold_first_product.store(enable ? 1 : 0); }
+bool withhold_first_product() { return g_withhold_first_product.load() != 0; }
 
 template <int D>
 static cudaError_t tc_fwd_d(const TcFwdArgs &A)

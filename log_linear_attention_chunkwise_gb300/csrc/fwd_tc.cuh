@@ -30,5 +30,6 @@ int tc_launches(int T);
 cudaError_t tc_fwd(const TcFwdArgs &A);
 // Test hook: withhold each tile's first product and shorten the waits.
 void tc_set_withhold_first_product(int enable);
+bool withhold_first_product();
 
 }  // namespace lla

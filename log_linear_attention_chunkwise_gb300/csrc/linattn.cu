@@ -1,5 +1,6 @@
 // Linear attention with one decay per head: how a call is cut into segments,
 // the scan that joins their states, and which kernels walk them.
+#include "fwd_tc.cuh"
 #include "launch.cuh"
 #include "linattn.cuh"
 #include "sm100.cuh"
@@ -197,6 +198,7 @@ void call_args(const Args &A, const Segments &c, LinWalk &W, Scan &S)
 {
     W.log_decay = A.log_decay; W.lens = A.lens; W.B = A.B; W.H = A.H; W.T = A.T; W.dt = A.dt;
     W.nseg = c.n; W.seg_tiles = c.tiles; W.device_error = A.device_error; W.stream = A.stream;
+    W.withhold = withhold_first_product() ? 1 : 0;
     S.log_decay = A.log_decay; S.lens = A.lens; S.H = A.H; S.T = A.T; S.nseg = c.n; S.seg_tiles = c.tiles;
     S.device_error = A.device_error;
 }

@@ -47,6 +47,7 @@ struct LinWalk {
     lla_dtype dt;
     int32_t *device_error;
     void *stream;
+    int withhold;            // test hook: the walk's scores and the state pass's products are not issued
 };
 
 // exp(ld * n) for n >= 0.  The product's rounding error is carried into the

@@ -46,8 +46,9 @@ using namespace sm100;
 constexpr int kTile = kLinTile;
 constexpr int kStages = 2;
 constexpr uint32_t kBlk = kTile * 128;      // a 64-column block of a 128-row bf16 tile
-constexpr uint32_t kWait = 1u << 22;        // bounded waits (about half a second with back-off)
-constexpr uint32_t kIssuerSpin = 1u << 23;  // the scores' issuer's polls
+constexpr uint32_t kWait = 1u << 18;        // bounded waits (about half a second: 1.7 us a poll)
+constexpr uint32_t kIssuerSpin = 1u << 22;  // the scores' issuer's polls
+constexpr uint32_t kGivenUp = 16;           // of a thread one of whose waits ran out
 constexpr int kRowWarps = 8, kStateWarps = 8;
 constexpr int kWalkThreads = (kRowWarps + kStateWarps + 4) * 32;
 constexpr int kLoadThread = (kRowWarps + kStateWarps) * 32, kStoreThread = kLoadThread + 2 * 32;  // roles 0 and 2
@@ -96,6 +97,11 @@ __device__ __forceinline__ void report(int32_t *err, int code)
 // needs the waiter's own step.  Everywhere else the next phase already needs
 // the waiter.
 // A wait that gives up reports, and the thread's later waits give up at once.
+// A thread that loads asks for no more then, nor where its last copy into the
+// same place has not landed, whose barrier still counts that one (others gave
+// up on it).  What a thread has in flight it waits for at the end, a whole
+// limit again; products are in order, and one that gave up issues a tile's only
+// after polls that take longer than they do.
 struct Waiter {
     int32_t *err;
     uint32_t limit;
@@ -103,8 +109,17 @@ struct Waiter {
     {
         if (!mbar_wait(bar, parity & 1, limit)) {
             report(err, code);
-            limit = 16;
+            limit = kGivenUp;
         }
+    }
+    __device__ __forceinline__ bool given_up() const { return limit == kGivenUp; }
+    __device__ __forceinline__ bool may_load(uint64_t *bar, uint32_t parity) const
+    {
+        return !given_up() && mbar_test(bar, parity & 1);
+    }
+    __device__ __forceinline__ void last(uint64_t *bar, uint32_t parity, int code)
+    {
+        if (!mbar_wait(bar, parity & 1, kWait)) report(err, code);
     }
 };
 
@@ -601,29 +616,32 @@ linattn_walk_kernel(const __grid_constant__ LinWalk W, const __grid_constant__ W
         }
     } else {
         const int role = warp - kRowWarps - kStateWarps;
-        if (lane != 0) {
+        if (lane != 0 || (W.withhold && role == 1)) {  // withheld: nothing is left in flight, the waits on S run out
         } else if (role == 0) {  // ---- loads of x and y, one tile ahead (z: with the output)
             // one place each: the next tile's rows are brought to L2 meanwhile, so that their load is short
             auto ahead = [&](const void *base, int n) {
                 if (n < tiles) prefetch_tile(base, J.dx, tile_start(n), bh, W.T);
             };
+            int nx = 0, ny = 0;  // the last tiles asked for
             for (int n = 0; n < tiles; n++) {
                 // y: S has been formed and the state warps have theirs; x: the state has been read out too
                 if (n > 0) {
                     wait(&s.bar_s[(n - 1) % kStages], (n - 1) / kStages, LLA_DEVERR_SYNC_TIMEOUT);
                     wait(&s.bar_yread, n - 1, LLA_DEVERR_SYNC_TIMEOUT);
-                    load_y(n);
+                    if (!wait.may_load(&s.bar_y, n - 1)) break;
+                    load_y(ny = n);
                 }
                 ahead(J.x, n + 1);
                 ahead(J.y, n + 1);
                 if (n > 0) {
                     wait(&s.bar_o2, n - 1, LLA_DEVERR_SYNC_TIMEOUT);
-                    load_x(n);
+                    if (!wait.may_load(&s.bar_x, n - 1)) break;
+                    load_x(nx = n);
                 }
             }
             // no copy is in flight when the CTA ends
-            wait(&s.bar_x, tiles - 1, LLA_DEVERR_COPY_TIMEOUT);
-            wait(&s.bar_y, tiles - 1, LLA_DEVERR_COPY_TIMEOUT);
+            wait.last(&s.bar_x, nx, LLA_DEVERR_COPY_TIMEOUT);
+            wait.last(&s.bar_y, ny, LLA_DEVERR_COPY_TIMEOUT);
         } else if (role == 1) {  // ---- the scores' products: S of the next tile and P Z of this one, as they can go
             auto scores = [&](int n) {
                 tc_fence_after_sync();
@@ -640,10 +658,10 @@ linattn_walk_kernel(const __grid_constant__ LinWalk W, const __grid_constant__ W
             for (int n = -1; n < tiles; n++) {
                 bool next = n + 1 < tiles, pz = n >= 0;
                 for (uint32_t polls = 0; next || pz; polls++) {
-                    const bool give_up = polls >= (wait.limit == kWait ? kIssuerSpin : 16u);
+                    const bool give_up = polls >= (wait.limit == kWait ? kIssuerSpin : kGivenUp);
                     if (give_up) {
                         report(W.device_error, LLA_DEVERR_SYNC_TIMEOUT);
-                        wait.limit = 16;
+                        wait.limit = kGivenUp;
                     }
                     if (polls > 0) __nanosleep(32);  // its polls take issue slots from the working warps
                     if (pz && (give_up || (mbar_test(&s.bar_scaled, n & 1) &&
@@ -661,8 +679,9 @@ linattn_walk_kernel(const __grid_constant__ LinWalk W, const __grid_constant__ W
                 }
             }
             // every product has completed when the tensor memory is freed
-            wait(&s.bar_o[(tiles - 1) % kStages], (tiles - 1) / kStages, LLA_DEVERR_SYNC_TIMEOUT);
+            wait.last(&s.bar_o[(tiles - 1) % kStages], (tiles - 1) / kStages, LLA_DEVERR_SYNC_TIMEOUT);
         } else if (role == 2) {  // ---- output tiles on their way out, and loads of z into the places they leave
+            int asked = min(kStages, tiles);
             for (int n = 0; n < tiles; n++) {
                 const int st = n % kStages;
                 wait(&s.bar_staged[st], n / kStages, LLA_DEVERR_SYNC_TIMEOUT);
@@ -672,10 +691,14 @@ linattn_walk_kernel(const __grid_constant__ LinWalk W, const __grid_constant__ W
                     tma_store_commit();
                     tma_store_wait_read();
                 }
-                if (n + kStages < tiles) load_z(n + kStages);
+                if (n + kStages < tiles) {
+                    if (!wait.may_load(&s.bar_z[st], n / kStages)) break;
+                    load_z(n + kStages);
+                    asked = n + kStages + 1;
+                }
             }
-            for (int n = max(0, tiles - kStages); n < tiles; n++)
-                wait(&s.bar_z[n % kStages], n / kStages, LLA_DEVERR_COPY_TIMEOUT);
+            for (int n = max(0, asked - kStages); n < asked; n++)
+                wait.last(&s.bar_z[n % kStages], n / kStages, LLA_DEVERR_COPY_TIMEOUT);
         } else {  // ---- the state's products: its read-out, then its update
             for (int n = 0; n < tiles; n++) {
                 const int st = n % kStages;
@@ -695,7 +718,7 @@ linattn_walk_kernel(const __grid_constant__ LinWalk W, const __grid_constant__ W
                 umma_commit(&s.bar_up[st]);
             }
             // every product has completed when the tensor memory is freed
-            wait(&s.bar_o2, tiles - 1, LLA_DEVERR_SYNC_TIMEOUT);
+            wait.last(&s.bar_o2, tiles - 1, LLA_DEVERR_SYNC_TIMEOUT);
         }
     }
     __syncwarp();
@@ -859,6 +882,7 @@ linattn_sum_kernel(const __grid_constant__ LinWalk W, const __grid_constant__ Wa
         }
     } else if (warp == kSumWarps) {
         if (lane == 0) {
+            int asked = min(kStages, tiles);
             for (int n = 0; n < tiles; n++) {
                 const int st = n % kStages;
                 // the tile after the next to L2: a stage is free only when its products are done
@@ -868,13 +892,15 @@ linattn_sum_kernel(const __grid_constant__ LinWalk W, const __grid_constant__ Wa
                 }
                 if (n >= kStages) {
                     wait(&s.bar_up[st], n / kStages - 1, LLA_DEVERR_SYNC_TIMEOUT);
+                    if (!wait.may_load(&s.bar_load[st], n / kStages - 1)) break;
                     load(n);
+                    asked = n + 1;
                 }
             }
-            for (int n = max(0, tiles - kStages); n < tiles; n++)
-                wait(&s.bar_load[n % kStages], n / kStages, LLA_DEVERR_COPY_TIMEOUT);
+            for (int n = max(0, asked - kStages); n < asked; n++)
+                wait.last(&s.bar_load[n % kStages], n / kStages, LLA_DEVERR_COPY_TIMEOUT);
         }
-    } else if (lane == 0) {
+    } else if (lane == 0 && !W.withhold) {  // withheld: nothing is left in flight, the waits on bar_up run out
         for (int n = 0; n < tiles; n++) {
             const int st = n % kStages;
             wait(&s.bar_parts[st], n / kStages, LLA_DEVERR_SYNC_TIMEOUT);
@@ -887,7 +913,7 @@ linattn_sum_kernel(const __grid_constant__ LinWalk W, const __grid_constant__ Wa
             mma_state_add<D>(acc, s.lo, s.z[st], false);
             umma_commit(&s.bar_up[st]);
         }
-        wait(&s.bar_up[(tiles - 1) % kStages], (tiles - 1) / kStages, LLA_DEVERR_SYNC_TIMEOUT);
+        wait.last(&s.bar_up[(tiles - 1) % kStages], (tiles - 1) / kStages, LLA_DEVERR_SYNC_TIMEOUT);
     }
     __syncwarp();
     tc_fence_before_sync();

@@ -84,3 +84,37 @@ def test_host_and_noalloc_entry_points_report_too():
         binding.debug_withhold_first_product(False)
     assert host_code == LLA_DEVERR_SYNC_TIMEOUT
     assert noalloc_code == LLA_DEVERR_SYNC_TIMEOUT
+
+
+@pytest.mark.parametrize("T,H,d", [(300, 2, 128), (300, 2, 64), (2000, 1, 128)])
+def test_withheld_products_of_linear_attention_are_reported(T, H, d):
+    """Whole walks with a state's pass behind them, and segments with the pass before them: both kinds of waits run
+    out, the call ends and reports, without a word too, and the calls after it are right."""
+    gen = torch.Generator().manual_seed(5)
+    q, k, v, do = (torch.randn((1, H, T, d), generator=gen).to(torch.bfloat16).cuda() / d ** 0.5 for _ in range(4))
+    ld = torch.full((H,), -0.02, device="cuda")
+    lens = torch.tensor([T - 3], dtype=torch.int32, device="cuda")
+
+    def calls(**kw):
+        return (binding.linattn_fwd(q, k, v, ld, lens=lens, return_state=True, **kw),
+                binding.linattn_bwd(q, k, v, ld, do, lens=lens, return_dstate=True, **kw))
+
+    want = calls()
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    binding.debug_withhold_first_product(True)
+    try:
+        codes = []
+        for one in (binding.linattn_fwd, lambda *a, **kw: binding.linattn_bwd(*a, do, **kw)):
+            err.zero_()
+            one(q, k, v, ld, lens=lens, device_error=err)
+            codes.append(binding.device_error_check(err))
+        calls()
+        torch.cuda.synchronize()
+    finally:
+        binding.debug_withhold_first_product(False)
+    assert codes == [LLA_DEVERR_SYNC_TIMEOUT] * 2
+    err.zero_()
+    got = calls(device_error=err)
+    assert binding.device_error_check(err) == 0
+    for g, w in zip(got, want):
+        assert all(torch.equal(a, b) for a, b in zip(g, w))
