@@ -35,8 +35,8 @@
  *   - Errors found while the kernels run.  The tensor-core kernels hand work
  *     between warps and copy engines through shared-memory barriers; every
  *     wait on one is bounded by a number of polls (about half a second in
- *     linear attention, seven in the others).  A wait that runs out
- *     records an lla_device_error code and the kernel carries on to its end
+ *     linear attention and layer norm, seven in the others).  A wait that
+ *     runs out records an lla_device_error code and the kernel carries on to its end
  *     (every later wait is bounded too), so the GPU never hangs; the output
  *     of that call is then invalid.  Entry points with such waits
  *     take `int32_t *device_error`: NULL, or one int32 of device memory owned
@@ -100,7 +100,9 @@ lla_status lla_device_error_check(const int32_t *device_error, int32_t *code, vo
  * out, LLA_DEVERR_SYNC_TIMEOUT is recorded and the launch finishes with an
  * invalid output.  Linear attention in bf16 likewise withholds the walk's
  * scores and the state pass's products; its waits keep their bounds, so that
- * such a call takes a second or two.  Process-wide; 0 restores normal operation. */
+ * such a call takes a second or two, and so does one of layer norm, whose
+ * CTAs withhold their first copy (LLA_DEVERR_COPY_TIMEOUT).  Process-wide;
+ * 0 restores normal operation. */
 void lla_debug_withhold_first_product(int enable);
 
 /* L = 1 + bit_length(T-1): lambda entries per token for a length-T forward

@@ -19,6 +19,7 @@
 // Measured: 16 heads of 32768 rows of 128, bf16, 268 MB, 51 us forward (5.2
 // TB/s; a device copy of the size reaches 6.2); the gradients of 2 x 16 heads
 // of 8192 such rows, 201 MB, 37 us; of 8192 rows of 2048, 101 MB, 28 us.
+#include "fwd_tc.cuh"
 #include "launch.cuh"
 #include "layer_norm.cuh"
 #include "sm100.cuh"
@@ -112,7 +113,9 @@ __device__ __forceinline__ void row_sum(float (&v)[M], float *red)
 // bytes in flight without holding them in registers.  Used where rows are whole
 // 16-byte pieces and a turn of all inputs fits kRingBytes at least twice.
 constexpr int kRingBytes = 40 * 1024;
-constexpr uint32_t kCopyWait = 1u << 22;  // bounded waits (about half a second with back-off)
+constexpr uint32_t kCopyWait = 1u << 18;  // bounded waits (about half a second: 1.7 us a poll)
+constexpr uint32_t kGivenUp = 16;         // of a CTA one of whose waits ran out,
+constexpr uint32_t kDrained = 15;         // and whose filling thread has seen to what was in flight
 
 template <int INPUTS, int TURN_BYTES>
 struct Ring {
@@ -120,26 +123,43 @@ struct Ring {
     static constexpr int kStages = kFit > 4 ? 4 : kFit;
     uint8_t data[kStages][INPUTS][TURN_BYTES];
     uint64_t bar[kStages];
+    volatile uint32_t limit;  // polls of a wait
 
     __device__ __forceinline__ void init()
     {
         if (threadIdx.x == 0) {
+            limit = kCopyWait;
             for (int i = 0; i < kStages; i++) sm100::mbar_init(&bar[i], 1);
             sm100::fence_mbar_init();
         }
         __syncthreads();
     }
-    // one thread: turn t's `bytes` of every input
+    // one thread: turn t's `bytes` of every input.  Not once a wait has run out: the barrier may still count the
+    // place's last copy.
     __device__ __forceinline__ void fill(int t, const void *const (&src)[INPUTS], uint32_t bytes)
     {
+        if (limit != kCopyWait) return;
         uint64_t *b = &bar[t % kStages];
         sm100::mbar_arrive_expect_tx(b, INPUTS * bytes);
         for (int k = 0; k < INPUTS; k++) sm100::bulk_load(data[t % kStages][k], src[k], bytes, b);
     }
     __device__ __forceinline__ void wait(int t, int32_t *err)
     {
-        if (!sm100::mbar_wait(&bar[t % kStages], (t / kStages) & 1, kCopyWait) && err != nullptr)
-            atomicCAS(err, 0, LLA_DEVERR_COPY_TIMEOUT);
+        if (!sm100::mbar_try_wait(&bar[t % kStages], (t / kStages) & 1)) wait_on(t, err);
+    }
+    // out of line, for the registers of the loops that wait
+    __device__ __noinline__ void wait_on(int t, int32_t *err)
+    {
+        if (sm100::mbar_wait(&bar[t % kStages], (t / kStages) & 1, limit)) return;
+        if (err != nullptr) atomicCAS(err, 0, LLA_DEVERR_COPY_TIMEOUT);
+        // Later waits are short.  The thread that fills waits here, once, for all that may be in flight (turns not
+        // asked for take their limit), so that none is when the CTA ends.
+        if (threadIdx.x == 0 && limit != kDrained) {
+            limit = kDrained;
+            for (int i = 0; i < kStages; i++, t++) sm100::mbar_wait(&bar[t % kStages], (t / kStages) & 1, kCopyWait);
+        } else if (limit == kCopyWait) {
+            limit = kGivenUp;
+        }
     }
 };
 
@@ -154,6 +174,7 @@ struct NormParams {
     int H, T, N, chunks;  // chunks: CTAs of one (batch, head)
     float eps;
     int32_t *err;
+    int withhold;         // test hook: the ring's first copy is not issued
 };
 
 // Rows of (b, h) that count: lens[b], T without lens; a length out of range is
@@ -203,7 +224,7 @@ layer_norm_fwd_kernel(const __grid_constant__ NormParams p)
         const long long r = lo + (long long)t * kTurn;
         const void *const src[1] = {x + r * N};
         if constexpr (kBulk)
-            if (r < hi) ring.fill(t, src, (uint32_t)(min((long long)kTurn, hi - r) * N * sizeof(T)));
+            if (r < hi && (t > 0 || !p.withhold)) ring.fill(t, src, (uint32_t)(min((long long)kTurn, hi - r) * N * sizeof(T)));
     };
     auto load = [&](long long r0, int t, P (&raw)[ROWS][ITEMS]) {
 #pragma unroll
@@ -323,8 +344,8 @@ layer_norm_bwd_kernel(const __grid_constant__ NormParams p)
     const int chunk = (int)(blockIdx.x % p.chunks);
     const int h = (int)(bh % p.H), b = (int)(bh / p.H);
     const int n = rows_of(p.lens, b, p.T, p.err);
-    const long long lo = chunk * p.rows_per_cta;
-    const long long hi = min((long long)n, lo + p.rows_per_cta);
+    const unsigned lo = (unsigned)(chunk * p.rows_per_cta);  // rows fit 32 bits, a turn beyond T too
+    const unsigned hi = (unsigned)min((long long)n, chunk * p.rows_per_cta + p.rows_per_cta);
     const int lane = threadIdx.x % TPR, grp = threadIdx.x / TPR;
     const int N = p.N, np = N / VEC;
     sm100::grid_launch_dependents();
@@ -346,24 +367,24 @@ layer_norm_bwd_kernel(const __grid_constant__ NormParams p)
     constexpr bool kBulk = VEC > 1 && 4 * kTurnBytes <= kRingBytes;
     __shared__ __align__(128) std::conditional_t<kBulk, Ring<2, kTurnBytes>, int> ring;
     [[maybe_unused]] auto fill = [&](int t) {
-        const long long r = lo + (long long)t * kTurn;
-        const void *const src[2] = {x + r * N, dy + r * N};
+        const unsigned r = lo + (unsigned)t * kTurn;
+        const void *const src[2] = {x + (long long)r * N, dy + (long long)r * N};
         if constexpr (kBulk)
-            if (r < hi) ring.fill(t, src, (uint32_t)(min((long long)kTurn, hi - r) * N * sizeof(T)));
+            if (r < hi && (t > 0 || !p.withhold)) ring.fill(t, src, (uint32_t)(min((unsigned)kTurn, hi - r) * N * (unsigned)sizeof(T)));
     };
     struct Rows {
         P x[ROWS][ITEMS], d[ROWS][ITEMS];
         float mu[ROWS], rs[ROWS];
     };
-    auto load_stats = [&](long long r0, Rows &t) {
+    auto load_stats = [&](unsigned r0, Rows &t) {
 #pragma unroll
         for (int q = 0; q < ROWS; q++) {
-            const long long r = r0 + q * kGroups + grp;
+            const unsigned r = r0 + q * kGroups + grp;
             t.mu[q] = r < hi ? mean[r] : 0.f;
             t.rs[q] = r < hi ? rstd[r] : 0.f;
         }
     };
-    auto load_rows = [&](long long r0, int n, Rows &t) {
+    auto load_rows = [&](unsigned r0, int n, Rows &t) {
 #pragma unroll
         for (int q = 0; q < ROWS; q++)
 #pragma unroll
@@ -376,8 +397,8 @@ layer_norm_bwd_kernel(const __grid_constant__ NormParams p)
                     t.x[q][i] = reinterpret_cast<const P *>(ring.data[n % ring.kStages][0])[k * np + c];
                     t.d[q][i] = reinterpret_cast<const P *>(ring.data[n % ring.kStages][1])[k * np + c];
                 } else {
-                    t.x[q][i] = reinterpret_cast<const P *>(x + (r0 + k) * N)[c];
-                    t.d[q][i] = reinterpret_cast<const P *>(dy + (r0 + k) * N)[c];
+                    t.x[q][i] = reinterpret_cast<const P *>(x + (long long)(r0 + k) * N)[c];
+                    t.d[q][i] = reinterpret_cast<const P *>(dy + (long long)(r0 + k) * N)[c];
                 }
             }
     };
@@ -391,7 +412,7 @@ layer_norm_bwd_kernel(const __grid_constant__ NormParams p)
     }
     load_stats(lo, t);
     int turn = 0, n_turn = 0;
-    for (long long r0 = lo; r0 < hi; r0 += kTurn, turn ^= 1, n_turn++) {
+    for (unsigned r0 = lo; r0 < hi; r0 += kTurn, turn ^= 1, n_turn++) {
         Rows next;  // on their way while these rows are worked on
         load_stats(r0 + kTurn, next);
         if constexpr (kBulk) {
@@ -431,7 +452,7 @@ layer_norm_bwd_kernel(const __grid_constant__ NormParams p)
         }
 #pragma unroll
         for (int q = 0; q < ROWS; q++) {
-            const long long r = r0 + q * kGroups + grp;
+            const unsigned r = r0 + q * kGroups + grp;
             if (r >= hi) continue;
             const float a = s[2 * q] * inv, c2 = s[2 * q + 1] * inv;
 #pragma unroll
@@ -447,7 +468,7 @@ layer_norm_bwd_kernel(const __grid_constant__ NormParams p)
                     // g rounded as in its sum: what cancels exactly (a row of one column) leaves nothing
                     o[e] = t.rs[q] * ((__fmul_rn(dv[e], w[i][e]) - a) - hh * c2);
                 }
-                reinterpret_cast<P *>(dx + r * N)[c] = pack<T, VEC>(o);
+                reinterpret_cast<P *>(dx + (long long)r * N)[c] = pack<T, VEC>(o);
             }
         }
         if constexpr (kBulk) {
@@ -607,6 +628,7 @@ NormParams params(const LayerNormArgs &A, const Variant &v, bool bwd)
     NormParams p{};
     p.x = A.x; p.dy = A.dy; p.weight = A.weight; p.bias = A.bias; p.lens = A.lens; p.y = A.y;
     p.mean = A.mean; p.rstd = A.rstd; p.H = A.H; p.T = A.T; p.N = A.N; p.eps = A.eps; p.err = A.device_error;
+    p.withhold = withhold_first_product() ? 1 : 0;
     split_rows(bwd ? v.bwd_turn : v.fwd_turn, A.B, A.H, A.T, bwd ? v.bwd_ctas : fwd_ctas(v),
                &p.rows_per_cta, &p.chunks);
     return p;

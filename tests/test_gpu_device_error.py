@@ -24,6 +24,7 @@ from parity import assert_parity
 
 pytestmark = pytest.mark.gpu
 
+LLA_DEVERR_COPY_TIMEOUT = 1
 LLA_DEVERR_SYNC_TIMEOUT = 2
 
 
@@ -118,3 +119,34 @@ def test_withheld_products_of_linear_attention_are_reported(T, H, d):
     assert binding.device_error_check(err) == 0
     for g, w in zip(got, want):
         assert all(torch.equal(a, b) for a, b in zip(g, w))
+
+
+@pytest.mark.parametrize("N,dtype", [(128, torch.bfloat16), (2048, torch.bfloat16), (128, torch.float32)])
+def test_withheld_copies_of_layer_norm_are_reported(N, dtype):
+    """A CTA of many turns (of widths that come in by bulk copies) whose first copy never comes: the call ends in a few
+    limits, not one a turn."""
+    gen = torch.Generator().manual_seed(5)
+    x, dy = (torch.randn((1, 1, 200000 if N < 2048 else 30000, N), generator=gen).to(dtype).cuda() for _ in range(2))
+    want, mean, rstd = binding.layer_norm_fwd(x, return_stats=True)
+    grads = binding.layer_norm_bwd(x, None, mean, rstd, dy)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    binding.debug_withhold_first_product(True)
+    try:
+        codes = []
+        for call in (lambda: binding.layer_norm_fwd(x, device_error=err),
+                     lambda: binding.layer_norm_bwd(x, None, mean, rstd, dy, device_error=err)):
+            err.zero_()
+            start = torch.cuda.Event(enable_timing=True)
+            end = torch.cuda.Event(enable_timing=True)
+            start.record()
+            call()
+            end.record()
+            codes.append(binding.device_error_check(err))
+            assert start.elapsed_time(end) < 20e3
+    finally:
+        binding.debug_withhold_first_product(False)
+    assert codes == [LLA_DEVERR_COPY_TIMEOUT] * 2
+    err.zero_()
+    assert torch.equal(binding.layer_norm_fwd(x, device_error=err), want)
+    got = binding.layer_norm_bwd(x, None, mean, rstd, dy, device_error=err)
+    assert binding.device_error_check(err) == 0 and all(torch.equal(a, b) for a, b in zip(got, grads))
