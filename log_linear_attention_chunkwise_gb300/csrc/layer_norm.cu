@@ -324,15 +324,17 @@ layer_norm_fwd_kernel(const __grid_constant__ NormParams p)
 
 // CTAs of the backward an SM holds: the fewest that keep enough bytes in flight,
 // since every CTA leaves a row of column sums for each gradient.  Three of 256
-// threads where a row stays within a warp and a thread has few of its values
-// (2 x 16 heads of 8192 rows of 128: 40 us with two, 37 with three, 113 with
-// four, whose registers no longer hold a turn), else 512 threads (8192 rows of
-// 2048: 28 us so, 33 with 768, 60 with 1024).
-template <int TPR, int VEC, int ITEMS, int THREADS>
-constexpr int kBwdCtas = TPR <= 32 && (VEC > 1 ? VEC * ITEMS <= 8 : ITEMS <= 4) ? 3 : (THREADS < 512 ? 512 / THREADS : 1);
+// threads where a row stays within a warp and a thread has 16 bytes of it (2 x
+// 16 heads of 8192 rows of 128, bf16: 40 us with two, 37 with three, 113 with
+// four, whose registers no longer hold a turn; with 32 bytes three no longer
+// hold one either: 131072 rows of 256, fp32, 154 us with three, 73 with two),
+// else 512 threads (8192 rows of 2048: 28 us so, 33 with 768, 60 with 1024).
+template <typename T, int TPR, int VEC, int ITEMS, int THREADS>
+constexpr int kBwdCtas =
+    TPR <= 32 && (VEC > 1 ? VEC * ITEMS * sizeof(T) <= 16 : ITEMS <= 4) ? 3 : (THREADS < 512 ? 512 / THREADS : 1);
 
 template <typename T, int VEC, int TPR, int ITEMS, int ROWS, int THREADS>
-__global__ void __launch_bounds__(THREADS, kBwdCtas<TPR, VEC, ITEMS, THREADS>)
+__global__ void __launch_bounds__(THREADS, kBwdCtas<T, TPR, VEC, ITEMS, THREADS>)
 layer_norm_bwd_kernel(const __grid_constant__ NormParams p)
 {
     using P = typename Pack<T, VEC>::type;
@@ -560,7 +562,7 @@ constexpr Variant variant()
     constexpr int kHeld = ITEMS * VEC;  // values of a row a thread holds
     constexpr int kRows = TPR > 32 ? (kHeld <= 8 && TPR < 1024 ? 2 : 1) : (kHeld <= 8 ? 4 : (kHeld <= 16 ? 2 : 1));
     constexpr int kRowsB = kHeld <= 8 && TPR < 1024 ? 2 : 1;
-    return {TPR * ITEMS * VEC, kThreads, kThreads / TPR * kRows, kThreads / TPR * kRowsB, kBwdCtas<TPR, VEC, ITEMS, kThreads>,
+    return {TPR * ITEMS * VEC, kThreads, kThreads / TPR * kRows, kThreads / TPR * kRowsB, kBwdCtas<T, TPR, VEC, ITEMS, kThreads>,
             layer_norm_fwd_kernel<T, VEC, TPR, ITEMS, kRows, kThreads>,
             layer_norm_bwd_kernel<T, VEC, TPR, ITEMS, kRowsB, kThreads>};
 }
@@ -592,9 +594,10 @@ template <> struct Variants<float> {
 
 // The narrowest variant that holds a row.  Rows whose length is no multiple of
 // a 16-byte piece go value by value (VEC = 1).
-// The widest of those keep 16 values a thread and spill a part of them; up to
-// 8192 columns have a variant of 8 and a row a turn (4000 rows of 5001, bf16: 92
-// and 333 us forward and backward in the wide one, 48 and 96 in this).
+// Above 8192 columns a thread keeps 16 values in 64 registers and spills a part
+// of them; odd widths up to there have a variant of 8 and a row a turn (4000 rows
+// of 5001, bf16: 92 and 333 us forward and backward in the wide one, 48 and 96 in
+// this).
 template <typename T>
 const Variant &pick(int N)
 {

@@ -229,3 +229,9 @@ def test_refusals(cuda_device):
         binding.layer_norm_fwd(torch.zeros(1, 1, 1, 16385, device="cuda"))
     with pytest.raises(ValueError, match="contiguous"):
         binding.layer_norm_fwd(torch.zeros(1, 2, 64, 3, device="cuda").transpose(2, 3))
+
+
+@pytest.mark.parametrize("B,H,T,N", [(1, 1, 20000, 132), (2, 3, 2100, 160), (1, 2, 9001, 252), (1, 1, 20000, 256), (3, 2, 17, 192)])
+def test_fp32_rows_of_two_pieces_a_thread(B, H, T, N, cuda_device):
+    """132 to 256 columns in single precision, many turns a CTA."""
+    test_fwd_and_bwd(B, H, T, N, F32, cuda_device)
