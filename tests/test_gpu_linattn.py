@@ -497,3 +497,33 @@ def test_decode_on_an_empty_pool(cuda_device):
     with pytest.raises(binding.LLAError, match="INVALID_ARGUMENT"):  # without slots every sequence needs a state
         binding.linattn_decode_step(torch.empty((0, 2, 64, 64), device="cuda"), *(x[n][:, :, 0].contiguous() for n in "qkv"),
                                     x["log_decay"])
+
+
+@pytest.mark.parametrize("dk,dv,dtype", [(16, 16, F32), (64, 32, BF16)])
+def test_decode_of_thousands_with_slots_named_twice(dk, dv, dtype, cuda_device):
+    B, H, pool = 5000, 2, 6000
+    x = lin_inputs(B, H, 1, dk, dv, dtype, seed=12)
+    gen = torch.Generator().manual_seed(13)
+    base = torch.randn((pool, H, dk, dv), generator=gen)
+    slots = torch.randperm(pool, generator=gen)[:B]
+    slots[[0, 4999]] = int(slots[2500])                    # one slot three times
+    slots[4097] = int(slots[129])                          # another one twice, far apart
+    slots[[7, 3333]] = -1
+    slots[[1000]] = pool
+    skip = torch.zeros(B, dtype=torch.bool)
+    skip[[0, 4999, 2500, 4097, 129, 7, 3333, 1000]] = True
+    state, err = base.cuda(), torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = binding.linattn_decode_step(state, *(x[n][:, :, 0].contiguous().cuda() for n in "qkv"), x["log_decay"].cuda(),
+                                      slots=slots.to(torch.int32).cuda(), device_error=err)
+    torch.cuda.synchronize()
+    assert int(err.item()) - 1 in (0, 4999, 2500, 4097, 129, 1000)
+    on = slots[~skip]
+    keep = {n: x[n][~skip] for n in "qkv"}
+    ax = absolute(keep)
+    ref = linattn(*(keep[n] for n in "qkv"), x["log_decay"], None, base[on])
+    wgt = linattn(*(ax[n] for n in "qkv"), x["log_decay"], None, base[on].abs())
+    assert_close(out[~skip.cuda()], ref[0][:, :, 0], wgt[0][:, :, 0], F32, dk, dv, 1, "out")
+    assert_close(state[on.cuda()], ref[1], wgt[1], F32, dk, dv, 1, "state")
+    rest = torch.ones(pool, dtype=torch.bool)
+    rest[on] = False
+    assert bool((out[skip.cuda()] == 0).all()) and torch.equal(state[rest.cuda()].cpu(), base[rest])
