@@ -235,3 +235,28 @@ def test_refusals(cuda_device):
 def test_fp32_rows_of_two_pieces_a_thread(B, H, T, N, cuda_device):
     """132 to 256 columns in single precision, many turns a CTA."""
     test_fwd_and_bwd(B, H, T, N, F32, cuda_device)
+
+
+def raw_bwd(x, w, mean, rstd, dy, dx, dw, db, ws):
+    """lla_layer_norm_bwd itself: outputs that may be absent or the same buffer as an input."""
+    p = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    B, H, T, N = x.shape
+    return binding.load().lla_layer_norm_bwd(
+        p(x), p(w), p(mean), p(rstd), None, p(dy), p(dx), p(dw), p(db), B, H, T, N, int(x.dtype == BF16), 0, p(ws),
+        0 if ws is None else ws.numel(), None, torch.cuda.current_stream().cuda_stream)
+
+
+@pytest.mark.parametrize("N,dtype", [(64, BF16), (256, F32), (999, BF16), (2048, F32)])
+def test_gradients_that_are_not_asked_for_and_in_place(N, dtype, cuda_device):
+    x, w, b, dy = (t.cuda() for t in inputs(2, 3, 40, N, dtype, seed=6))
+    _, mean, rstd = binding.layer_norm_fwd(x, w, b, return_stats=True)
+    dx, dw, db = binding.layer_norm_bwd(x, w, mean, rstd, dy)
+    ws = torch.empty(1 << 24, dtype=torch.uint8, device="cuda")
+    for names in ((), ("dw",), ("db",), ("dw", "db")):
+        got = {n: torch.full_like(dw, 7.0) for n in names}
+        for into in ("new", "dy", "x"):
+            gx, gdy, gin = torch.full_like(x, 7.0), dy.clone(), x.clone()
+            gx = {"new": gx, "dy": gdy, "x": gin}[into]
+            assert raw_bwd(gin, w, mean, rstd, gdy, gx, got.get("dw"), got.get("db"), ws if names else None) == 0
+            assert torch.equal(gx, dx)
+            assert all(torch.equal(g, {"dw": dw, "db": db}[n]) for n, g in got.items())

@@ -527,3 +527,26 @@ def test_decode_of_thousands_with_slots_named_twice(dk, dv, dtype, cuda_device):
     rest = torch.ones(pool, dtype=torch.bool)
     rest[on] = False
     assert bool((out[skip.cuda()] == 0).all()) and torch.equal(state[rest.cuda()].cpu(), base[rest])
+
+
+@pytest.mark.parametrize("T,H,dtype", [(300, 2, BF16), (1700, 1, BF16), (1700, 1, F32)])
+@pytest.mark.parametrize("bad", [-1, None])
+def test_sequences_beside_a_bad_length_are_right(T, H, dtype, bad, cuda_device):
+    """All rows and states of the other sequences, forward and backward, at the bounds of every other test."""
+    d = 64
+    x = lin_inputs(3, H, T, d, d, dtype, seed=14)
+    h, ax = dev(x), absolute(x)
+    bad = T + 1 if bad is None else bad
+    lens = torch.tensor([T, bad, T // 2], dtype=torch.int32, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    args = [h[n] for n in ("q", "k", "v", "log_decay")]
+    got = binding.linattn_fwd(*args, lens=lens, state_in=h["state"], return_state=True, device_error=err) + \
+        binding.linattn_bwd(*args, h["dout"], lens=lens, state_in=h["state"], dstate_out=h["dstate"], return_dstate=True,
+                            device_error=err)
+    assert binding.device_error_check(err) == 3
+    good = [T, 0, T // 2]
+    both = [linattn(u["q"], u["k"], u["v"], x["log_decay"], good, u["state"]) +
+            linattn_grads(u["q"], u["k"], u["v"], x["log_decay"], u["dout"], good, u["state"], u["dstate"]) for u in (x, ax)]
+    for name, g, r, w in zip(("out", "state", "dq", "dk", "dv", "dstate"), got, *both):
+        assert bool((g[1] == 0).all()), name  # the skipped one, in outputs made by the call
+        assert_close(g[[0, 2]], r[[0, 2]], w[[0, 2]], F32 if "state" in name else dtype, d, d, T, name)
