@@ -442,6 +442,8 @@ def _launch(stream, call):
     belongs to that stream."""
     if stream is None:
         return call(torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()))
+    if stream.device.index != torch._C._cuda_getDevice():  # it would make its own device the current one
+        raise ValueError(f"the stream is on {stream.device}, expected the tensors' device")
     with torch.cuda.stream(stream):
         return call(stream.cuda_stream)
 

@@ -246,3 +246,12 @@ def test_decode_overlaps_are_refused(lib):
             assert dec(out=p) == ARG, base
     for base in (2, 3, 4):
         assert dec(state=at(base)) == ARG and dec(state=at(base, 256)) == ARG
+
+
+def test_a_stream_of_another_device_is_refused(monkeypatch):
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    stream = type("Stream", (), {"device": torch.device("cuda", 1), "cuda_stream": 16})()
+    called = []
+    with pytest.raises(ValueError, match="stream is on cuda:1"):
+        binding._launch(stream, called.append)
+    assert not called
