@@ -16,9 +16,10 @@
 // go to the workspace and a second kernel adds them in a fixed order, so
 // repeated calls give the same bits.
 //
-// Measured: 16 heads of 32768 rows of 128, bf16, 268 MB, 51 us forward (5.2
-// TB/s; a device copy of the size reaches 6.2); the gradients of 2 x 16 heads
-// of 8192 such rows, 201 MB, 37 us; of 8192 rows of 2048, 101 MB, 28 us.
+// Measured, whole calls: 16 heads of 32768 rows of 128, bf16, 268 MB, 52 us
+// forward (5.2 TB/s; a device copy of the size reaches 6.2); the gradients of 2 x
+// 16 heads of 8192 such rows, 201 MB, 39 us; of 8192 rows of 2048, 101 MB, 30 us.
+// The figures further down compare variants with one another.
 #include "fwd_tc.cuh"
 #include "launch.cuh"
 #include "layer_norm.cuh"
@@ -56,7 +57,6 @@ __device__ __forceinline__ typename Pack<T, VEC>::type pack(const float (&x)[VEC
 }
 
 // VEC fp32 values of a [N] vector at column c, or `other` without a vector.
-// `wide`: 16-byte loads (N a multiple of 4 and VEC too).
 template <int VEC>
 __device__ __forceinline__ void load_param(const float *p, int c, float other, float (&x)[VEC])
 {
@@ -610,8 +610,8 @@ const Variant &pick(int N)
 }
 
 // CTAs of one (batch, head) and the rows of each: at most `per_sm` CTAs per SM
-// over the grid (one more would wait for a whole CTA to end) and at least one
-// turn each.
+// over the grid and at least one turn each.  Backward that is what an SM holds (a
+// CTA more would wait for a whole one to end and leave another row of sums).
 void split_rows(int turn, int B, int H, int T, int per_sm, long long *rows_per_cta, int *chunks)
 {
     const long long bh = (long long)B * H;
@@ -622,8 +622,8 @@ void split_rows(int turn, int B, int H, int T, int per_sm, long long *rows_per_c
     *chunks = (int)(((long long)T + *rows_per_cta - 1) / *rows_per_cta);
 }
 
-// Threads of a full SM; the registers hold 768, so that the rest of the grid fills the places of CTAs that have
-// ended (65536 rows of 2048: 95 us so, 100 with 768 threads' CTAs).
+// Forward, threads of a full SM: more than the registers hold (768), on purpose: the rest of the grid fills the
+// places of CTAs that have ended (65536 rows of 2048: 95 us so, 100 with 768 threads' CTAs).
 int fwd_ctas(const Variant &v) { return 2048 / v.threads; }
 
 NormParams params(const LayerNormArgs &A, const Variant &v, bool bwd)

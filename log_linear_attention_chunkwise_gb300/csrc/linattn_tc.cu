@@ -29,9 +29,10 @@
 // neither chain of products waits for the other's.  Shared memory holds the
 // state operand, both parts, x, y and two stages of z, 32 KB each at D = 128.
 //
-// Measured: 16 heads of 32768 tokens, D = 128, in 9 segments each 115 us for
-// 537 MB (4.7 TB/s; the state pass before it 61 us for 268 MB); 128 whole walks
-// of 2500 tokens 72 us; the gradients' 96 whole walks of 8192 tokens 196 us.
+// Measured: 16 heads of 32768 tokens, D = 128, in 9 segments each 102 us for
+// 537 MB (5.3 TB/s; the state pass before it 61 us for 268 MB; the call 169);
+// 128 whole walks of 2500 tokens 72 us; the gradients' 96 whole walks of 8192
+// tokens 196 us.
 // The simple kernel on the CUDA cores took 2322 us for the first, state and all.
 #include "launch.cuh"
 #include "linattn.cuh"
