@@ -36,9 +36,9 @@
  *     between warps and copy engines through shared-memory barriers; every
  *     wait on one is bounded by a number of polls (about half a second in
  *     linear attention and layer norm, seven in the others).  A wait that
- *     runs out records an lla_device_error code and the kernel carries on to its end
- *     (every later wait is bounded too), so the GPU never hangs; the output
- *     of that call is then invalid.  Entry points with such waits
+ *     runs out records an lla_device_error code and the kernel carries on to
+ *     its end (every later wait is bounded too), so the GPU never hangs; the
+ *     output of that call is then invalid.  Entry points with such waits
  *     take `int32_t *device_error`: NULL, or one int32 of device memory owned
  *     by the caller that the kernels set (atomically, first code wins) and
  *     never clear.  Zero it before the calls it should cover and read it
@@ -496,7 +496,8 @@ lla_status lla_linattn_bwd(const void *q, const void *k, const void *v, const fl
  *   columns of a head, hidden by the states' bytes up to about a thousand
  *   sequences (at 65535 of one head, d = 128, seven times their time).
  * state and out overlap neither each other nor q, k, v (refused).
- * Supported: dk, dv in {16,32,64,128}; B <= 65535; pool, H >= 0.
+ * Supported: dk, dv in {16,32,64,128}; B <= 65535; pool, H >= 0 (an empty pool
+ * may have no address).
  */
 lla_status lla_linattn_decode_step(float *state, const void *q, const void *k, const void *v,
                                    const float *log_decay, const int32_t *slots, float *out,
@@ -527,11 +528,12 @@ lla_status lla_zero_padding(void *const *rows, const int32_t *row_bytes, const i
  *     dx = rstd (g - avg(g) - h avg(g h)),  dweight = sum over b, t of dy h,
  *     dbias = sum over b, t of dy.
  *   mean, rstd as the forward wrote them; dx [B,H,T,N] in dt, may be the same
- *   buffer as dy or x; dweight, dbias [H,N] fp32, nullable, overwritten; sums in a
- *   fixed order (the same bits every time).
+ *   buffer as dy or x; dweight, dbias [H,N] fp32, nullable, overwritten; sums
+ *   in a fixed order (the same bits every time).
  * Supported: 1 <= N <= 16384, B*H <= 65535, any T >= 0, eps >= 0.  x, dy, y,
  * dx, weight, bias 16-byte aligned.  Beyond the buffers that may be the same,
- * no output overlaps another one or an input (refused).  Empty calls write zero dweight and dbias.
+ * no output overlaps another one or an input (refused).  Empty calls write zero
+ * dweight and dbias.
  */
 lla_status lla_layer_norm_fwd(const void *x, const float *weight, const float *bias,
                               const int32_t *lens, void *y, float *mean, float *rstd, int B, int H,

@@ -61,10 +61,11 @@ struct Cost {
 // How a call runs.  Its walks (`walks` of them, counted in heads) go over whole
 // sequences, or in segments side by side whose incoming states `passes` state
 // passes and the scan form first: the cheapest cut into at most kLinMaxSeg
-// segments of whole tiles (more where bf16 walks of kLinWalkTiles need them).  A state that is handed out (`state`) comes with
-// split walks from the scan.  Whole walks in fp32 hand it out themselves;
-// those in bf16, whose own state is only as accurate as their output, leave it
-// to one state pass behind them.
+// segments of whole tiles (more where bf16 walks of at most kLinWalkTiles need
+// them).  A state that is handed out (`state`) comes with split walks from the
+// scan.  Whole walks in fp32 hand it out themselves; those in bf16, whose own
+// state is only as accurate as their output, leave it to one state pass behind
+// them.
 struct Plan {
     Segments cut;
     size_t part;  // bytes of one pass's states
